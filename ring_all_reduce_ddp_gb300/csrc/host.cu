@@ -33,6 +33,12 @@ ddp_status alloc_device(void** ptr, size_t bytes, const char* what) {
   return fail(DDP_ERR_NOMEM, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
+ddp_status upload(void* dst, const void* src, size_t bytes, const char* what) {
+  DDP_CUDA(cudaMemcpy(dst, src, bytes, cudaMemcpyHostToDevice), what);
+  DDP_CUDA(cudaStreamSynchronize(cudaStreamLegacy), what);
+  return DDP_OK;
+}
+
 ddp_status cuda_fail(cudaError_t e, const char* where) {
   t_error = std::string(where) + ": " + cudaGetErrorString(e);
   return DDP_ERR_CUDA;

@@ -65,6 +65,11 @@ struct Plan;
 ddp_status alloc_async(void** ptr, size_t bytes, cudaStream_t s, const char* what);
 // The same for a handle's long-lived memory (cudaMalloc).
 ddp_status alloc_device(void** ptr, size_t bytes, const char* what);
+// Copy host memory to the device; the bytes are there when it returns. A copy
+// from pageable memory alone may return once the bytes are staged, and no
+// launch on a non-blocking stream is ordered behind the legacy stream that
+// carries it: what a kernel on any stream may read next takes this way.
+ddp_status upload(void* dst, const void* src, size_t bytes, const char* what);
 
 ddp_status fail(ddp_status s, const std::string& msg);
 ddp_status cuda_fail(cudaError_t e, const char* where);

@@ -87,10 +87,10 @@ ddp_status build_table(const std::vector<OptimTensor>& recs, int elems, const vo
   std::memcpy(host.data() + o_tile0, tile0.data(), (k + 1) * sizeof(int32_t));
   void* mem = nullptr;
   DDP_TRY(alloc_device(&mem, total, "optim tile table"));
-  const cudaError_t e = cudaMemcpy(mem, host.data(), total, cudaMemcpyHostToDevice);
-  if (e != cudaSuccess) {
-    cudaFree(mem);
-    return cuda_fail(e, "optim tile table upload");
+  const ddp_status st = upload(mem, host.data(), total, "optim tile table upload");
+  if (st != DDP_OK) {
+    (void)cudaFree(mem);
+    return st;
   }
   unsigned char* d = static_cast<unsigned char*>(mem);
   out->mem = mem;
