@@ -143,7 +143,7 @@ ddp_status build_reducer_table(ddp_reducer* h) {
   void* mem = nullptr;
   DDP_TRY(alloc_device(&mem, total, "reducer piece table"));
   h->table_mem = mem;
-  DDP_CUDA(cudaMemcpy(mem, host.data(), total, cudaMemcpyHostToDevice), "reducer piece table upload");
+  DDP_TRY(upload(mem, host.data(), total, "reducer piece table upload"));
   unsigned char* d = static_cast<unsigned char*>(mem);
   h->table.ptr = reinterpret_cast<void* const*>(d + o_ptr);
   h->table.start = reinterpret_cast<const int64_t*>(d + o_start);

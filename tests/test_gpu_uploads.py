@@ -72,3 +72,25 @@ def test_create_is_ordered_before_a_norm_on_another_stream():
     side.synchronize()
     want = oo.norms(M.g.host)[0]
     assert abs(float(norm) - want) <= 33 * U * want
+
+
+@pytest.mark.parametrize("buffers", [False, True])
+def test_a_reducer_is_made_before_its_step_on_another_stream(buffers):
+    """Integers: every sum is exact, whatever its order."""
+    import ring_all_reduce_ddp_gb300 as D
+    p, sizes = 4, [5000, 1, 0, 70001, 33]
+    g = torch.Generator().manual_seed(53)
+    grads = [[torch.randint(-99, 100, (n,), generator=g).float().cuda() for n in sizes] for _ in range(p)]
+    bufs = [[torch.full((77,), float(r), device="cuda")] for r in range(p)]
+    want = [sum(grads[r][j] for r in range(p)) for j in range(len(sizes))]
+    side = torch.cuda.Stream()
+    busy = Busy()
+    red = D.DDPReducer(grads)
+    assert busy.done()
+    if buffers:
+        red.set_buffers(bufs, root=1)
+    red.step(1.0, stream=side)
+    side.synchronize()
+    for r in range(p):
+        assert all(torch.equal(grads[r][j], want[j]) for j in range(len(sizes)))
+        assert bool((bufs[r][0] == (1.0 if buffers else r)).all())
