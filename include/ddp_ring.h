@@ -525,7 +525,8 @@ ddp_status ddp_optim_norm(ddp_optim* handle, ddp_norm kind, float* norm, float* 
  *   replicas' gradients, replica 0's being the handle's own.
  * All outputs are written whatever c is. A NaN norm gives NaN everywhere, an
  * infinite one zeros (NaN where the gradient is infinite), as the formula does.
- * max_norm must be positive; infinity means that nothing is clipped.
+ * max_norm must be positive; infinity means that nothing is clipped: c is 1,
+ * under an infinite norm too (a NaN norm still gives NaN).
  * DDP_ERR_STATE before outputs are set. */
 ddp_status ddp_optim_set_outputs(ddp_optim* handle, int32_t p, void* const* outs);
 ddp_status ddp_optim_clip(ddp_optim* handle, ddp_norm kind, float max_norm, float* norm, cudaStream_t stream);

@@ -26,9 +26,12 @@ def norms(grads, kind: str = "l2"):
 
 
 def coefficient(norm: float, max_norm: float) -> float:
-    """min(1, max_norm / (norm + 1e-6)); a NaN stays one."""
+    """min(1, max_norm / (norm + 1e-6)); a NaN stays one. An infinite max_norm
+    clips nothing, whatever the norm: 1."""
     if math.isnan(norm):
         return norm
+    if math.isinf(max_norm):
+        return 1.0
     return min(1.0, max_norm / (norm + CLIP_EPS))
 
 
