@@ -431,7 +431,11 @@ ddp_status ddp_reducer_step(ddp_reducer* handle, float divisor, cudaStream_t str
  *   If the rebuild fails after the old buckets were released (an allocation
  *   returns DDP_ERR_NOMEM), the handle keeps no buckets and no device memory:
  *   ddp_reducer_sync, _prepare and _mark_ready then return DDP_ERR_STATE
- *   until a rebuild succeeds; destroy works as always. */
+ *   until a rebuild succeeds; destroy works as always.
+ * ddp_reducer_rebuild, ddp_reducer_set_buffers and ddp_reducer_destroy free
+ *   tables (and the flat buckets, but for set_buffers) that a launch captured
+ *   into a graph holds by address: a graph captured before one of them must
+ *   not be replayed after it. */
 ddp_status ddp_reducer_prepare(ddp_reducer* handle);
 /* The grid of the bucket launches ddp_reducer_mark_ready fires: max_blocks
  * == 0 (the default) gives one block per 2 KB tile; max_blocks > 0 at most
@@ -486,7 +490,12 @@ ddp_status ddp_reduce_scatter_noalloc(const void* const* in, void* const* out, i
  * replicas. Norm, coefficient and step count stay on the device: no call
  * below waits for it, except ddp_optim_create, the two set calls (they upload
  * tables, and replacing one drains the device) and ddp_optim_destroy; the
- * others only launch kernels, and may be captured into a graph.
+ * others only launch kernels, and may be captured into a graph. A captured
+ * launch holds the address of the handle's table, which the next
+ * ddp_optim_set_outputs frees for ddp_optim_clip, the next
+ * ddp_optim_set_params for ddp_optim_adamw, and ddp_optim_destroy for every
+ * call: a graph captured before one of these must not be replayed after it,
+ * but captured again. A replay is a call on the handle.
  *
  * ddp_optim_create plans the launches over one gradient set.
  *   grads[k]: device pointers (kept, not copied, until destroy), numel[k]

@@ -325,7 +325,9 @@ def ddp_bucket_allreduce(grads, numel, offset, dtype=DDP_FLOAT32, divisor: float
 
 
 class DDPReducer:
-    """ddp_reducer_create / sync / destroy: a whole gradient synchronisation per call."""
+    """ddp_reducer_create / sync / destroy: a whole gradient synchronisation per call.
+    set_buffers, rebuild and destroy free tables that a launch captured into a
+    CUDA graph holds: such a graph must not be replayed after one of them."""
 
     def __init__(self, grads, first_bucket_cap_bytes: int = 1 << 20, bucket_cap_bytes: int = 25 << 20,
                  order: int = DDP_ORDER_REVERSED):
@@ -422,7 +424,10 @@ class DDPOptim:
     """ddp_optim_create / norm / clip / adamw / destroy: the global norm of one
     replica's gradients, clipping into p replicas, and the AdamW update of p
     replicas' parameters. `norm` is a float32 device tensor of one element, which
-    every call leaves on the device. The tensors are kept alive by the handle."""
+    every call leaves on the device. The tensors are kept alive by the handle.
+    norm, clip and adamw may be captured into a CUDA graph; set_outputs ends the
+    validity of graphs that captured clip, set_params of those with adamw,
+    destroy of all: capture them again, a replay would read freed memory."""
 
     h = None
 
