@@ -442,8 +442,12 @@ class DDPOptim:
                                       _dtype(grads[0].dtype) if grads else DDP_FLOAT32))
         self.h = h
         # The stream calls default to: the current one of the gradients' device,
-        # as a handle (0.1 us; torch.cuda.current_stream() builds an object in 3 us).
-        self._current = functools.partial(torch._C._cuda_getCurrentRawStream, grads[0].device.index)
+        # as a handle (0.1 us; torch.cuda.current_stream() builds an object in
+        # 3 us, and serves a torch without the raw accessor).
+        device = grads[0].device.index
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._current = (functools.partial(raw, device) if raw
+                         else lambda: int(torch.cuda.current_stream(device).cuda_stream))
 
     def _on(self, stream):
         return self._current() if stream is None else _stream(stream)
