@@ -12,12 +12,13 @@
  * Conventions (every call):
  *   - Pointer arrays (bufs, in, out, grads, tensors, bucket) are HOST arrays of
  *     DEVICE pointers. They are read during the call and not kept, except by a
- *     ddp_ring handle, which keeps a copy until ddp_ring_destroy.
+ *     ddp_ring, ddp_reducer or ddp_optim handle, which keeps a copy until it is
+ *     destroyed (or the pointers are set again).
  *   - The caller owns every replica, input and output buffer. The library
  *     allocates only:
  *       a handle's device memory, freed by its destroy call: a ddp_ring's
  *       workspace; a ddp_reducer's flat buckets, piece table, buffer table and
- *       workspace;
+ *       workspace; a ddp_optim's tile tables and workspace;
  *       stream-ordered temporaries (cudaMallocAsync / cudaFreeAsync on the
  *       caller's stream) for the literal schedules of one-shot calls, the
  *       persistent ring's step flags, and the fp32 workspace of the bf16
@@ -28,7 +29,9 @@
  *     finalize_backward"). Only these wait for the device: ddp_ring_sync,
  *     ddp_device_error, ddp_reducer_create (its piece-table upload),
  *     ddp_reducer_set_buffers (its table upload),
- *     ddp_reducer_rebuild (drains the device first), the destroy calls, and
+ *     ddp_reducer_rebuild (drains the device first), ddp_optim_create,
+ *     ddp_optim_set_outputs and ddp_optim_set_params (their table uploads;
+ *     replacing a table drains the device), the destroy calls, and
  *     every collective while the call log (DDP_RING_LOG) is on.
  *   - Threads: calls on different handles, or handle-free calls, may run
  *     from several host threads at once. One handle must not be used from
@@ -85,7 +88,7 @@ typedef enum {
   DDP_ERR_ARG = 1,            /* bad argument (null pointer, range, aliasing)      */
   DDP_ERR_DTYPE = 2,          /* unsupported or mismatched element type            */
   DDP_ERR_NOT_DIVISIBLE = 3,  /* torch-contract reduce_scatter with p not dividing n */
-  DDP_ERR_ALIGN = 4,          /* reserved                                          */
+  DDP_ERR_ALIGN = 4,          /* a pointer is not aligned to its element size       */
   DDP_ERR_NOMEM = 5,          /* a device allocation failed                        */
   DDP_ERR_CUDA = 6,           /* a CUDA call or launch failed                      */
   DDP_ERR_TIMEOUT = 7,        /* a bounded device-side wait gave up                */

@@ -87,8 +87,9 @@ __device__ __forceinline__ void store8(__nv_bfloat16* at, const float* f) {
 // V consecutive elements at any address: a gradient that is a view at an odd
 // offset of a flat bucket, while the other streams keep their vectors. Lanes
 // overlap in the lines they read, so these loads do fill L1. ResNet-50-shaped
-// set, 8 replicas: update 208.6 us with aligned gradients and with misaligned
-// ones (297.8 with every stream element by element), bf16 clip 83.8 and 85.8 us.
+// set, 8 replicas, aligned gradients and misaligned ones: update 210.6 and 211.1
+// us in fp32, 143.0 and 143.5 in bf16 (297.8 in fp32 with every stream element by
+// element), clip 161.0 and 161.6, in bf16 85.3 and 87.8.
 template <int V, typename T>
 __device__ __forceinline__ void load_each(const T* at, float* f) {
 #pragma unroll
@@ -256,9 +257,12 @@ __device__ __forceinline__ int32_t block_of_tile(int32_t ntiles, int32_t blocks,
 // Llama-1B-shaped bf16 set (2.4 GB): 20.3 and 333-337 us (7.2 TB/s, 1.06 of the
 // measured copy rate); blocks striding over the tiles 24.8 and 358 us, and with
 // no loads ahead 27.4 and 386; 8 KB tiles at 6 or 8 blocks per SM 24-25 and
-// 350-383 us; 3 blocks per SM 22.4 and 348; 5 and more spill. Tiles handed out
-// from a counter for the last 10-50 % of the set change nothing (22.4-23.5 and 333-336
-// against 22.9 and 338).
+// 350-383 us; 3 blocks per SM 22.4 and 348. At 4 the bf16 sum of squares fills
+// its 64 registers and spills 4 bytes (20 with EACH), at 5 up to 114; the other
+// forms spill nothing at 4. Tiles handed out from a counter for the last 10-50 %
+// of the set change nothing (22.4-23.5 and 333-336 against 22.9 and 338); that
+// was not tried on sets of many ragged tiles, where blocks of equal tile counts
+// differ by up to a quarter in bytes from their mean.
 template <typename T, bool INF, bool EACH>
 __global__ void __launch_bounds__(kNormThreads, kNormBlocksPerSm)
     k_optim_norm(const OptimTable t, const OptimWork w, float* norm) {
@@ -407,7 +411,8 @@ __device__ __forceinline__ float clip_coefficient(float norm, float max_norm) {
 // tile, LOADS vectors per thread. Of the clip of the ResNet-50-shaped set into
 // 8 replicas this part takes 138 us (920 MB, 6.65 TB/s), of the GPT-2-shaped
 // bf16 set into 2 116 us (747 MB, 6.4 TB/s). Writing the tile with bulk stores
-// from shared memory took the same time within 2 %.
+// from shared memory took the same time within 2 %. With two vectors in bf16 a
+// thread spills 8 bytes; the other forms none.
 // The gradients come from HBM a second time: the coefficient depends on all
 // of them. Visiting the tiles in reverse, or those read last first, and marking
 // the replicas' writes evict-first gained at most 3 us of 159, and marking the
